@@ -227,13 +227,17 @@ __device__ __forceinline__ void fp4_item(const Fp4Params& p, const int32_t* it, 
   if (kOne || hr < G) {
     const uint4* qv = reinterpret_cast<const uint4*>(
         p.q + ((size_t)d * p.Hq + (size_t)g * G + (kOne ? 0 : hr)) * HD + qd * (HD / 4));
+    const auto to_f16 = [](uint32_t two) {
+      const float a = bf16lo(two), b = bf16hi(two);
+      return pack_f16x2(f16_range(a, a), f16_range(b, b));
+    };
 #pragma unroll
     for (int j = 0; j < kSteps / 2; ++j) {
       const uint4 w = qv[j];
-      qb[2 * j][0] = pack_f16x2_sat(bf16lo(w.x), bf16hi(w.x));
-      qb[2 * j][1] = pack_f16x2_sat(bf16lo(w.y), bf16hi(w.y));
-      qb[2 * j + 1][0] = pack_f16x2_sat(bf16lo(w.z), bf16hi(w.z));
-      qb[2 * j + 1][1] = pack_f16x2_sat(bf16lo(w.w), bf16hi(w.w));
+      qb[2 * j][0] = to_f16(w.x);
+      qb[2 * j][1] = to_f16(w.y);
+      qb[2 * j + 1][0] = to_f16(w.z);
+      qb[2 * j + 1][1] = to_f16(w.w);
     }
     if constexpr (kOne) {
 #pragma unroll

@@ -1203,14 +1203,18 @@ __device__ bool decode_tc_fp8(const Params& p, const CUtensorMap* tmk, const CUt
     const uint4* qv = reinterpret_cast<const uint4*>(
         p.q_decode + ((size_t)d * p.Hq + (size_t)g * G + hr) * 128 + 32 * qd);
     const float4* kv = reinterpret_cast<const float4*>(p.k_scale + (size_t)g * 128 + 32 * qd);
+    const auto scaled = [](uint32_t two, float lo, float hi) {
+      const float a = bf16lo(two), b = bf16hi(two);
+      return pack_f16x2(f16_range(a * lo, a), f16_range(b * hi, b));
+    };
 #pragma unroll
     for (int j = 0; j < 4; ++j) {  // 8 channels per uint4: k-steps 2j and 2j + 1
       const uint4 w = qv[j];
       const float4 s0 = kv[2 * j], s1 = kv[2 * j + 1];
-      qa0[2 * j] = pack_f16x2_sat(bf16lo(w.x) * s0.x, bf16hi(w.x) * s0.y);
-      qa2[2 * j] = pack_f16x2_sat(bf16lo(w.y) * s0.z, bf16hi(w.y) * s0.w);
-      qa0[2 * j + 1] = pack_f16x2_sat(bf16lo(w.z) * s1.x, bf16hi(w.z) * s1.y);
-      qa2[2 * j + 1] = pack_f16x2_sat(bf16lo(w.w) * s1.z, bf16hi(w.w) * s1.w);
+      qa0[2 * j] = scaled(w.x, s0.x, s0.y);
+      qa2[2 * j] = scaled(w.y, s0.z, s0.w);
+      qa0[2 * j + 1] = scaled(w.z, s1.x, s1.y);
+      qa2[2 * j + 1] = scaled(w.w, s1.z, s1.w);
     }
   }
   float ot[kKS][4];  // Oᵀ: channels 16hr + 2mt (+1) x heads 2qd, 2qd+1

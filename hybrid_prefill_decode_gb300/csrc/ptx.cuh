@@ -425,9 +425,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// As pack_f16x2, with magnitudes above the f16 range clamped to its largest finite value.
-__device__ __forceinline__ uint32_t pack_f16x2_sat(float lo, float hi) {
-  return pack_f16x2(fmaxf(fminf(lo, kF16Max), -kF16Max), fmaxf(fminf(hi, kF16Max), -kF16Max));
+// x within the f16 range (larger magnitudes become its largest finite value), and NaN where `of`, the
+// number that x was made from, is NaN or infinite: `of` times 0 is that NaN, and 0 otherwise. (The
+// clamp alone would return its bound for a NaN.)
+__device__ __forceinline__ float f16_range(float x, float of) {
+  return fmaf(of, 0.f, fmaxf(fminf(x, kF16Max), -kF16Max));
 }
 // Word i (0-3) of a uint4; i must be a compile-time constant after unrolling.
 __device__ __forceinline__ uint32_t u4_word(const uint4& v, int i) {

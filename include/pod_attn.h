@@ -249,7 +249,8 @@ pod_attn_status pod_attn_run_append(pod_attn_plan_t plan, const void* q_prefill,
  * channel c = e4m3(v_pool8[..][j][c]) * v_scale[..][j]. The query and output stay bf16.
  * Arithmetic: e4m3 is converted to f16 exactly; q * k_scale and the softmax weights times
  * v_scale are rounded to f16 for the tensor cores (magnitudes above 65504 saturate there);
- * scores, softmax and accumulation are fp32.
+ * scores, softmax and accumulation are fp32. A NaN or an infinity in a query head makes that head's
+ * outputs NaN, as the formula does.
  *   plan          : a plan made with options.kv_fp8 set, no prefill sequences and head_dim 128
  *                   (else UNSUPPORTED); its variant is not used: the work runs as one launch.
  *   q_decode, o_decode : device bf16 [Nd][Hq][128], as pod_attn_run.
@@ -413,10 +414,11 @@ pod_attn_status pod_attn_rope_append(pod_attn_plan_t plan, pod_attn_rope_t rope,
 /* ---------------------------------------------------------------- the 4-bit cache
  * Decode attention over an E2M1 cache, head dim 128 or 64: pod_attn_run's decode with the cached
  * rows' values as defined above. q is rounded to f16 for the tensor cores (exact for magnitudes from
- * 2^-14 to 65504; larger ones saturate), code * scale byte is exact in f16, the softmax weights (with
- * one query head per kv-head also their products with V's scale bytes) are rounded to f16; scores,
- * softmax statistics and accumulation are fp32. A cached NaN (scale byte
- * 0x7F) in a visible row makes its sequence's outputs NaN where the formula does.
+ * 2^-14 to 65504; larger finite ones saturate), code * scale byte is exact in f16, the softmax weights
+ * (with one query head per kv-head also their products with V's scale bytes) are rounded to f16;
+ * scores, softmax statistics and accumulation are fp32. A NaN or an infinity in a query head makes
+ * that head's outputs NaN, and a cached NaN (scale byte 0x7F) in a visible row its sequence's outputs
+ * where the formula does.
  *   plan  : a plan made with options.kv_fp4 and no prefill sequences (else UNSUPPORTED); its variant
  *           is not used: the work runs as one launch.
  *   cache : type E2M1 (else UNSUPPORTED); num_blocks as in the plan's problem (else INVALID_ARG).

@@ -95,6 +95,22 @@ def test_fp8_bad_block_index_is_reported_not_faulted():
     assert_close(B.decode_fp8(ok.to("cuda")), oracle.decode_fp8(ok), "fp8 after bad index")
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("hq,hkv,lens", [(4, 4, [1, 40]), (16, 2, [17, 4000])])
+def test_fp8_decode_of_a_query_that_is_not_finite(hq, hkv, lens, bad):
+    """Its head has no softmax and gives NaN; the other heads do not change by a bit."""
+    fb = W.make_fp8_decode_batch(hq, hkv, lens, seed=hq).to("cuda")
+    clean = B.decode_fp8(fb)
+    for seq, head, ch in ((0, 0, 0), (1, hq - 1, 127), (1, hq // 2, 67)):
+        keep = fb.q_decode.clone()
+        fb.q_decode[seq, head, ch] = bad
+        o = B.decode_fp8(fb)
+        fb.q_decode.copy_(keep)
+        assert torch.isnan(o[seq, head]).all()
+        o[seq, head] = clean[seq, head]
+        assert torch.equal(o, clean)
+
+
 @pytest.mark.parametrize("cfg", [2, 3, 4])
 def test_fp8_full_size_decodes_of_each_configuration(cfg):
     """The decodes the benchmark times (--kv-fp8 --config cfg), in its launch configuration
