@@ -354,7 +354,7 @@ pod_attn_status build_plan(const pod_attn_problem& prob, const int32_t* cu, cons
   std::vector<DUnit> du;
   int64_t total = 0;
   double pf = 0, pb = 0, db = 0, df = 0;
-  const double row_bytes = 4.0 * Hkv * D;  // K + V, bf16
+  const double row_bytes = (double)(Hkv * kv_row_bytes(opt, D));
   const bool causal = opt.non_causal == 0;
   for (int s = 0; s < Np; ++s) {
     const int64_t q = (int64_t)cu[s + 1] - cu[s], L = kv[s], P = L - q;

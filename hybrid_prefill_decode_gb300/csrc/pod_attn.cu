@@ -1893,16 +1893,16 @@ pod_attn_status pod_attn_plan_bucket(pod_attn_plan_t plan, pod_attn_bucket* out)
   const pod_attn_problem& pr = plan->prob;
   const int Np = pr.num_prefill_seqs, Nd = pr.num_decode_seqs;
   const int64_t hd = pr.head_dim;
-  const int64_t row = 4 * hd;  // K + V (or q + o) of one row, bf16
+  const int64_t kv_row = kv_row_bytes(plan->opt, hd), qo_row = 4 * hd;  // K and V; q and o in bf16
   int64_t flops = 0, bytes = 0;
   for (int s = 0; s < Np; ++s) {
     const int64_t q = plan->cu[s + 1] - plan->cu[s], L = plan->kv[s], P = L - q;
     flops += 4 * hd * (int64_t)pr.num_q_heads *
              (plan->opt.non_causal == 0 ? q * P + q * (q + 1) / 2 : q * L);
-    bytes += L * pr.num_kv_heads * row + q * pr.num_q_heads * row;
+    bytes += L * pr.num_kv_heads * kv_row + q * pr.num_q_heads * qo_row;
   }
   for (int d = 0; d < Nd; ++d)
-    bytes += (int64_t)plan->kv[Np + d] * pr.num_kv_heads * row + (int64_t)pr.num_q_heads * row;
+    bytes += (int64_t)plan->kv[Np + d] * pr.num_kv_heads * kv_row + (int64_t)pr.num_q_heads * qo_row;
   auto bit_length = [](int64_t x) { int b = 0; while (x > 0) { ++b; x >>= 1; } return b; };
   auto bucket = [&](int64_t x, int64_t unit) { return x > 0 ? bit_length((x + unit - 1) / unit) : 0; };
   pod_attn_bucket r{};

@@ -187,6 +187,12 @@ struct pod_attn_plan_s {
 };
 
 namespace pod {
+// Bytes of one cached row of a kv-head, K and V with the scales that are stored per row, in the cache
+// that a plan is for: bf16; e4m3 with an fp32 scale per V row; e2m1 with an e4m3 scale per 16 channels.
+inline int64_t kv_row_bytes(const pod_attn_options& opt, int64_t head_dim) {
+  return opt.kv_fp4 ? 2 * (head_dim / 2 + head_dim / 16) : opt.kv_fp8 ? 2 * head_dim + 4 : 4 * head_dim;
+}
+
 // Planner entry (planner.cpp). Fills everything but cuda_state. num_sms must be > 0.
 pod_attn_status build_plan(const pod_attn_problem& prob, const int32_t* cu, const int32_t* kv,
                            const pod_attn_options& opt, int num_sms, pod_attn_plan_s* plan);

@@ -147,7 +147,8 @@ typedef struct {
   uint64_t workspace_bytes;   /* same as pod_attn_workspace_bytes */
   double est_prefill_flops;   /* algorithmic FLOPs: 4*d*Hq per visible (query, key) pair */
   double est_prefill_bytes;   /* algorithmic bytes: K/V once per kv-head, Q in, O out */
-  double est_decode_bytes;    /* algorithmic bytes: every cached K/V row once, q in, o out */
+  double est_decode_bytes;    /* algorithmic bytes: every cached K/V row of the plan's cache type
+                                 once, q in, o out */
   double est_decode_flops;
 } pod_attn_plan_info;
 
@@ -531,9 +532,9 @@ pod_attn_status pod_attn_get_plan_info(pod_attn_plan_t plan, pod_attn_plan_info*
  * batches give equal buckets, bit for bit. */
 typedef struct {
   int64_t prefill_flops;     /* 4*D*Hq per visible (query, key) pair of the prefill chunks */
-  int64_t read_bytes;        /* algorithmic bytes: each sequence's K/V rows once per kv-head
-                                (4*D B per row and kv-head), q in and o out (4*D B per token and
-                                q-head) */
+  int64_t read_bytes;        /* algorithmic bytes: each sequence's K/V rows once per kv-head (per
+                                row and kv-head 4*D B; kv_fp8 2*D + 4 B, kv_fp4 9*D/8 B), q in
+                                and o out (4*D B per token and q-head) */
   int32_t prefill_ctas;      /* virtual prefill CTAs (work items) */
   int32_t decode_ctas;       /* virtual decode CTAs */
   int32_t grid;              /* hardware CTAs of the fused launch */

@@ -57,6 +57,19 @@ def test_plan_bucket_matches_restatement(seed):
     assert b["tmem_cols_per_cta"] == (512 if q_lens else 0)
 
 
+@pytest.mark.parametrize("cache,hd,row", [({}, 128, 512), ({}, 64, 256), (dict(kv_fp8=True), 128, 260),
+                                          (dict(kv_fp4=True), 128, 144), (dict(kv_fp4=True), 64, 72)])
+def test_bytes_are_those_of_the_plan_s_cache(cache, hd, row):
+    """Per row and kv-head: bf16 2 * 2 bytes a channel; e4m3 2 * 1 and the V row's fp32 scale; e2m1
+    2 * 1/2 and 2 * 1/16 of e4m3 scales. q and o are bf16 in every plan."""
+    lens, hq, hkv = [8192] * 63 + [5], 32, 8
+    p = B.Plan(hq, hkv, [], lens, len(lens), 10, 512, 0.1, num_sms=152, head_dim=hd, **cache)
+    want = sum(lens) * hkv * row + len(lens) * hq * 4 * hd
+    b = p.bucket()
+    assert b["read_bytes"] == want == p.info()["est_decode_bytes"]
+    assert b["bucket_bytes"] == (-(-want // (1 << 20))).bit_length()
+
+
 def _table_with(entries):
     t = C.CostTable(32, 8, 152)
     for (q_lens, pkv, dkv), times in entries:
