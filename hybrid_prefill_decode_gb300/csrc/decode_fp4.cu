@@ -562,18 +562,34 @@ cudaError_t launch_fp4(const Fp4Params& p, int grid, cudaStream_t st) {
                       fp4_smem<GT, HD>(), st, p);
 }
 
+// Heads that the kernel of a group of G heads has room for.
+constexpr int fp4_group(int G) { return G <= 2 ? G : G <= 4 ? 4 : kMaxGroup; }
+
 template <int HD, int GW, bool kLevels>
 cudaError_t launch_fp4(const Fp4Params& p, int grid, cudaStream_t st) {
-  switch (p.G) {
+  switch (fp4_group(p.G)) {
     case 1: return launch_fp4<1, HD, GW, kLevels>(p, grid, st);
     case 2: return launch_fp4<2, HD, GW, kLevels>(p, grid, st);
-    case 3:
     case 4: return launch_fp4<4, HD, GW, kLevels>(p, grid, st);
-    default: return launch_fp4<8, HD, GW, kLevels>(p, grid, st);
+    default: return launch_fp4<kMaxGroup, HD, GW, kLevels>(p, grid, st);
   }
 }
 
 }  // namespace
+
+int fp4_smem_bytes(int group, int head_dim) {
+  const auto of = [&](auto gt) {
+    constexpr int GT = decltype(gt)::value;
+    return head_dim == 64 ? fp4_smem<GT, 64>() : fp4_smem<GT, 128>();
+  };
+  switch (fp4_group(group)) {
+    case 1: return of(std::integral_constant<int, 1>{});
+    case 2: return of(std::integral_constant<int, 2>{});
+    case 4: return of(std::integral_constant<int, 4>{});
+    default: return of(std::integral_constant<int, kMaxGroup>{});
+  }
+}
+
 }  // namespace pod
 
 using namespace pod;

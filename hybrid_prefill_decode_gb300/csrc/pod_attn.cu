@@ -1911,7 +1911,7 @@ pod_attn_status pod_attn_plan_bucket(pod_attn_plan_t plan, pod_attn_bucket* out)
   r.prefill_ctas = (int32_t)(plan->items_p.size() / kItemWords);
   r.decode_ctas = (int32_t)(plan->items_d.size() / kItemWords);
   r.grid = plan->grid_fused;
-  r.smem_per_cta = kSmemTotal;
+  r.smem_per_cta = plan_smem_bytes(*plan);
   r.tmem_cols_per_cta = r.prefill_ctas > 0 ? kTmemCols : 0;
   r.bucket_flops = bucket(flops, int64_t(1) << 30);
   r.bucket_bytes = bucket(bytes, int64_t(1) << 20);
@@ -1933,8 +1933,8 @@ pod_attn_status pod_attn_get_plan_info(pod_attn_plan_t plan, pod_attn_plan_info*
   r.grid_fused = plan->grid_fused;
   r.grid_prefill = plan->grid_prefill;
   r.grid_decode = plan->grid_decode;
-  r.smem_bytes = kSmemTotal;
-  r.threads_per_cta = kThreads;
+  r.smem_bytes = plan_smem_bytes(*plan);
+  r.threads_per_cta = plan_threads(*plan);
   r.item_words = kItemWords;
   r.workspace_bytes = plan->ws.total;
   r.est_prefill_flops = plan->est_prefill_flops;

@@ -197,6 +197,14 @@ inline int64_t kv_row_bytes(const pod_attn_options& opt, int64_t head_dim) {
 pod_attn_status build_plan(const pod_attn_problem& prob, const int32_t* cu, const int32_t* kv,
                            const pod_attn_options& opt, int num_sms, pod_attn_plan_s* plan);
 
+// Threads and dynamic shared memory of a CTA of the kernel that a plan's work runs in: the 4-bit decode's
+// (decode_fp4.cu) or the attention kernel's.
+int fp4_smem_bytes(int group, int head_dim);
+inline int plan_threads(const pod_attn_plan_s& p) { return p.opt.kv_fp4 ? kFp4Warps * 32 : kThreads; }
+inline int plan_smem_bytes(const pod_attn_plan_s& p) {
+  return p.opt.kv_fp4 ? fp4_smem_bytes(p.group, p.prob.head_dim) : kSmemTotal;
+}
+
 // Argument checks that the entry points share.
 inline pod_attn_status check_workspace(const pod_attn_plan_s* plan, const void* ws, size_t bytes) {
   if (!ws) return POD_ATTN_ERR_INVALID_ARG;

@@ -141,7 +141,8 @@ typedef struct {
   int32_t grid_fused;         /* CTAs of the fused launch */
   int32_t grid_prefill;       /* CTAs of the prefill-only launch (serial / streams) */
   int32_t grid_decode;        /* CTAs of the decode-only launch (serial / streams) */
-  int32_t smem_bytes;         /* dynamic shared memory per CTA (one budget for both kinds) */
+  int32_t smem_bytes;         /* dynamic shared memory per CTA (one budget for both kinds; kv_fp4:
+                                 of the 4-bit decode's CTA) */
   int32_t threads_per_cta;
   int32_t item_words;         /* int32 words per work item in pod_attn_plan_items' output */
   uint64_t workspace_bytes;   /* same as pod_attn_workspace_bytes */

@@ -70,6 +70,22 @@ def test_bytes_are_those_of_the_plan_s_cache(cache, hd, row):
     assert b["bucket_bytes"] == (-(-want // (1 << 20))).bit_length()
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("group,room", [(1, 1), (2, 2), (3, 4), (4, 4), (5, 8), (8, 8)])
+def test_shared_memory_of_4_bit_plans_is_their_kernel_s(hd, group, room):
+    """16 warps with two slots of 2 * blocks units of 9 * hd bytes each; per four warps a row of 132 floats
+    for each warp and head that the kernel has room for, or the 8 * 16 + 8 floats of a merge if they are
+    more, in 128-byte steps; then barriers and flags, less than 1 KiB."""
+    p = B.Plan(2 * group, 2, [], [900], 1, 99, 60, 0.1, num_sms=8, head_dim=hd, kv_fp4=True)
+    rings = 16 * 2 * 2 * {128: 2, 64: 4}[hd] * 9 * hd
+    scratch = 4 * -(-4 * max(4 * room * 132, 136) // 128) * 128
+    inf, b = p.info(), p.bucket()
+    assert rings + scratch < inf["smem_bytes"] < rings + scratch + 1024
+    assert b["smem_per_cta"] == inf["smem_bytes"] and inf["threads_per_cta"] == 512
+    bf16 = B.Plan(2 * group, 2, [], [900], 1, 99, 60, 0.1, num_sms=8, head_dim=hd).info()
+    assert inf["smem_bytes"] < bf16["smem_bytes"]
+
+
 def _table_with(entries):
     t = C.CostTable(32, 8, 152)
     for (q_lens, pkv, dkv), times in entries:
