@@ -69,7 +69,7 @@ class Bucket(ctypes.Structure):
                 ("grid", ctypes.c_int32), ("smem_per_cta", ctypes.c_int32),
                 ("tmem_cols_per_cta", ctypes.c_int32), ("bucket_flops", ctypes.c_int32),
                 ("bucket_bytes", ctypes.c_int32), ("bucket_ctas", ctypes.c_int32),
-                ("intensity", ctypes.c_double)]
+                ("intensity", ctypes.c_double), ("kv_type", ctypes.c_int32)]
 
 
 class ItemRecord(ctypes.Structure):

@@ -14,8 +14,9 @@ alongside). `calibrate` runs the fused kernel through the C ABI on seeded synthe
 records per bucket the p50 and p99 of the measured µs per iteration (cold L2), keeping the worst
 figures when several batches fall in one bucket. `lookup` returns the validated entry of a
 plan's bucket, or None when that bucket was never measured (outside the validated range: the
-caller decides); `choose_chunk` returns the largest candidate prefill chunk whose validated p99
-fits a time budget next to a given decode batch.
+caller decides). Caches of e4m3 and of 4-bit values run in other kernels, so the cache's type is
+part of the key: their plans find only what was added for them. `choose_chunk` returns the largest
+candidate prefill chunk whose validated p99 fits a time budget next to a given decode batch.
 
 Command line (on a GPU): python -m hybrid_prefill_decode_gb300.costtable --help
 """
@@ -29,12 +30,14 @@ from typing import Dict, Iterable, List, Optional, Sequence, Tuple
 
 from . import binding as B
 
-Key = Tuple[int, int]
+Key = Tuple[int, int, int]
 
 
 def key_of(bucket: dict) -> Key:
-    """The table key of a bucket: (prefill-FLOP bucket, bytes-read bucket)."""
-    return (int(bucket["bucket_flops"]), int(bucket["bucket_bytes"]))
+    """The table key of a bucket: (prefill-FLOP bucket, bytes-read bucket, cache type, one of
+    binding.KV_TYPES' values; 0: bf16)."""
+    return (int(bucket["bucket_flops"]), int(bucket["bucket_bytes"]),
+            int(bucket.get("kv_type", B.KV_TYPES["bf16"])))
 
 
 @dataclass
@@ -57,11 +60,14 @@ class CostTable:
     """Per-bucket validated latencies of one model shape (q-heads, kv-heads) on one GPU."""
 
     def __init__(self, num_q_heads: int, num_kv_heads: int, num_sms: int,
-                 entries: Optional[Dict[Key, Entry]] = None):
+                 entries: Optional[Dict[Tuple[int, ...], Entry]] = None):
         self.num_q_heads = num_q_heads
         self.num_kv_heads = num_kv_heads
         self.num_sms = num_sms
-        self.entries: Dict[Key, Entry] = dict(entries or {})
+        # a key without a cache type is of the bf16 cache
+        self.entries: Dict[Key, Entry] = {
+            (k[0], k[1], k[2] if len(k) > 2 else B.KV_TYPES["bf16"]): e
+            for k, e in (entries or {}).items()}
 
     # ---- building -----------------------------------------------------------------------
     def add(self, bucket: dict, times_us: Sequence[float]) -> None:
@@ -114,7 +120,8 @@ class CostTable:
     def to_json(self) -> str:
         return json.dumps({"num_q_heads": self.num_q_heads, "num_kv_heads": self.num_kv_heads,
                            "num_sms": self.num_sms,
-                           "entries": [{"bucket_flops": k[0], "bucket_bytes": k[1], **asdict(e)}
+                           "entries": [{"bucket_flops": k[0], "bucket_bytes": k[1], "kv_type": k[2],
+                                        **asdict(e)}
                                        for k, e in sorted(self.entries.items())]}, indent=1)
 
     @classmethod
@@ -122,7 +129,8 @@ class CostTable:
         d = json.loads(text)
         entries = {}
         for e in d["entries"]:
-            k = (int(e.pop("bucket_flops")), int(e.pop("bucket_bytes")))
+            k = (int(e.pop("bucket_flops")), int(e.pop("bucket_bytes")),
+                 int(e.pop("kv_type", B.KV_TYPES["bf16"])))
             entries[k] = Entry(**e)
         return cls(d["num_q_heads"], d["num_kv_heads"], d["num_sms"], entries)
 

@@ -1917,6 +1917,7 @@ pod_attn_status pod_attn_plan_bucket(pod_attn_plan_t plan, pod_attn_bucket* out)
   r.bucket_bytes = bucket(bytes, int64_t(1) << 20);
   r.bucket_ctas = bit_length((int64_t)r.prefill_ctas + r.decode_ctas);
   r.intensity = bytes > 0 ? (double)flops / (double)bytes : 0.0;
+  r.kv_type = plan->opt.kv_fp4 ? POD_ATTN_KV_E2M1 : plan->opt.kv_fp8 ? POD_ATTN_KV_E4M3 : POD_ATTN_KV_BF16;
   *out = r;
   return POD_ATTN_OK;
 }

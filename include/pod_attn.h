@@ -545,6 +545,8 @@ typedef struct {
   int32_t bucket_bytes;      /* 0 without work, else bit length of ceil(read_bytes / 2^20) */
   int32_t bucket_ctas;       /* bit length of prefill_ctas + decode_ctas */
   double intensity;          /* prefill_flops / read_bytes (FLOP per byte) */
+  int32_t kv_type;           /* pod_attn_kv_type of the plan's cache: latencies of one type say
+                                nothing about another's kernel */
 } pod_attn_bucket;
 
 /* Fill `out` for `plan`. Errors: INVALID_ARG (null plan or out). */

@@ -116,3 +116,37 @@ def test_buckets_keep_their_worst_figures_and_round_trip_json():
     t2 = C.CostTable.from_json(t.to_json())
     assert t2.entries == t.entries and (t2.num_q_heads, t2.num_kv_heads, t2.num_sms) == (32, 8, 152)
     json.loads(t.to_json())
+
+
+def test_other_caches_have_entries_of_their_own():
+    """The same batch over three caches: three kernels, three entries, wherever their buckets fall."""
+    lens = [8192] * 64
+    plans = {n: B.Plan(32, 8, [], lens, 64, 10, 512, 0.1, num_sms=152, **kw)
+             for n, kw in (("bf16", {}), ("e4m3", dict(kv_fp8=True)), ("e2m1", dict(kv_fp4=True)))}
+    assert [p.bucket()["kv_type"] for p in plans.values()] == \
+        [B.KV_TYPES[n] for n in plans] == [0, 1, 2]
+    t = C.CostTable(32, 8, 152)
+    # a bf16 batch in the bucket of bytes that the 4-bit plan falls in
+    small = B.Plan(32, 8, [], [2304] * 64, 64, 10, 512, 0.1, num_sms=152)
+    assert small.bucket()["bucket_bytes"] == plans["e2m1"].bucket()["bucket_bytes"]
+    for p in (plans["bf16"], small):
+        t.add(p.bucket(), [400.0] * 3)
+    assert t.lookup(plans["bf16"]).p99_us == 400.0
+    assert t.lookup(plans["e4m3"]) is None and t.lookup(plans["e2m1"]) is None
+    t.add(plans["e2m1"].bucket(), [90.0] * 3)
+    t = C.CostTable.from_json(t.to_json())
+    assert t.lookup(plans["e2m1"]).p99_us == 90.0 and t.lookup(small).p99_us == 400.0
+
+
+def test_tables_without_cache_types_are_of_the_bf16_cache():
+    p = B.Plan(32, 8, [], [8192] * 64, 64, 10, 512, 0.1, num_sms=152)
+    b, e = p.bucket(), C.Entry(1.0, 2.0, 3, 1, 0, 4, 0.0)
+    key = (b["bucket_flops"], b["bucket_bytes"])
+    assert C.CostTable(32, 8, 152, {key: e}).lookup(p) == e
+    d = json.loads(C.CostTable(32, 8, 152, {key: e}).to_json())
+    del d["entries"][0]["kv_type"]
+    assert C.CostTable.from_json(json.dumps(d)).lookup(p) == e
+    del b["kv_type"]
+    t = C.CostTable(32, 8, 152)
+    t.add(b, [5.0])
+    assert t.lookup(p).p50_us == 5.0
