@@ -273,8 +273,9 @@ def _rows(name, t, shape, index):
 
 
 class Rope:
-    """Rotary frequencies (pod_attn_rope_create): `scaling` is one of ROPE_SCALINGS; "custom" takes
-    `inv_freq`, one frequency per pair in radians per position. attention_factor 0: the default."""
+    """Rotary frequencies (pod_attn_rope_create): `scaling` is one of ROPE_SCALINGS; "custom", and no
+    other, takes `inv_freq`, one frequency per pair in radians per position. attention_factor 0: the
+    default."""
 
     def __init__(self, rot_dim: int, theta: float = 10000.0, interleaved: bool = False,
                  scaling: str = "none", factor: float = 1.0, original_max_position: float = 0.0,
@@ -284,6 +285,8 @@ class Rope:
         self.handle = None
         freq = None
         if inv_freq is not None:
+            if scaling != "custom":
+                raise ValueError(f"inv_freq: scaling {scaling!r} computes its own; want \"custom\"")
             if len(inv_freq) != rot_dim // 2:
                 raise ValueError(f"inv_freq: want {rot_dim // 2} values, got {len(inv_freq)}")
             freq = (ctypes.c_double * max(1, len(inv_freq)))(*[float(x) for x in inv_freq])

@@ -343,6 +343,13 @@ def test_rope_refusals(lib, kw):
     assert e.value.code == B.ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("kw", [
+    dict(), dict(scaling="linear", factor=4.0), dict(scaling="yarn", factor=2.0, original_max_position=64)])
+def test_rope_refuses_frequencies_that_it_would_not_use(lib, kw):
+    with pytest.raises(ValueError):
+        B.Rope(8, inv_freq=[.5, .25, .125, .1], **kw)
+
+
 def test_rope_custom_refuses_values_that_are_not_finite(lib):
     with pytest.raises(B.PodAttnError):
         B.Rope(4, scaling="custom", inv_freq=[1.0, float("inf")])
