@@ -612,7 +612,7 @@ extern "C" pod_attn_status pod_attn_run_decode_fp4(pod_attn_plan_t plan, const v
   if (!q_decode || !o_decode || !d_block_tables || !d_kv_lens || !cache->k_pool || !cache->v_pool ||
       !cache->k_scale || !cache->v_scale || cache->num_blocks != pr.num_blocks)
     return POD_ATTN_ERR_INVALID_ARG;
-  if (!aligned16({q_decode, o_decode, cache->k_pool, cache->v_pool, cache->k_scale, cache->v_scale}))
+  if (!aligned16({q_decode, o_decode}) || !cache_aligned(*cache))
     return POD_ATTN_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const WorkspaceLayout& w = plan->ws;

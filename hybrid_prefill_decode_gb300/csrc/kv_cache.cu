@@ -508,8 +508,7 @@ pod_attn_status pod_attn_rope_append(pod_attn_plan_t plan, pod_attn_rope_t rope,
       !d_block_tables || (scaled && (!cache->k_scale || !cache->v_scale)))
     return POD_ATTN_ERR_INVALID_ARG;
   if (q && ((Tp > 0 && !q_prefill) || (Nd > 0 && !q_decode))) return POD_ATTN_ERR_INVALID_ARG;
-  if (!aligned16({q, k_new, v_new, cache->k_pool, cache->v_pool, cache->k_scale, cache->v_scale,
-                  q_prefill, q_decode}))
+  if (!aligned16({q, k_new, v_new, q_prefill, q_decode}) || !cache_aligned(*cache))
     return POD_ATTN_ERR_INVALID_ARG;
   if ((q && (q_stride < q_row || q_stride % 8)) || k_stride < kv_row || k_stride % 8 ||
       v_stride < kv_row || v_stride % 8)
@@ -616,7 +615,7 @@ pod_attn_status pod_attn_expand_fp4(pod_attn_plan_t plan, const pod_attn_kv_cach
   if (!cache->k_pool || !cache->v_pool || !cache->k_scale || !cache->v_scale || cache->num_blocks < 1 ||
       !k_pool || !v_pool || !d_block_tables4 || !d_block_tables || !d_kv_lens)
     return POD_ATTN_ERR_INVALID_ARG;
-  if (!aligned16({cache->k_pool, cache->v_pool, cache->k_scale, cache->v_scale, k_pool, v_pool}))
+  if (!aligned16({k_pool, v_pool}) || !cache_aligned(*cache))
     return POD_ATTN_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   ExpandArgs a{};

@@ -217,6 +217,13 @@ inline bool aligned16(std::initializer_list<const void*> ptrs) {
   for (const void* p : ptrs) all |= reinterpret_cast<uintptr_t>(p);
   return (all & 15) == 0;
 }
+// Alignment of a cache's pools and scales: 16 bytes, but for the 4-bit cache's scales, single floats that
+// may be the rows of a table of all layers.
+inline bool cache_aligned(const pod_attn_kv_cache& c) {
+  const bool floats = c.type == POD_ATTN_KV_E2M1;
+  const uintptr_t scales = reinterpret_cast<uintptr_t>(c.k_scale) | reinterpret_cast<uintptr_t>(c.v_scale);
+  return aligned16({c.k_pool, c.v_pool}) && (scales & (floats ? 3 : 15)) == 0;
+}
 // The rules of pod_attn_copy_blocks (pages.cpp).
 pod_attn_status check_copies(const pod_attn_block_pool* pools, int32_t n_pools, int32_t num_blocks,
                              const int32_t* pairs, int32_t n_pairs);

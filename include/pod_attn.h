@@ -305,7 +305,7 @@ pod_attn_status pod_attn_append_fp8(pod_attn_plan_t plan, const void* k_new, con
  *          2i + 1 in the high four bits of byte i), then D scale bytes, for K [16 rows][D / 16
  *          groups] and for V [D / 16 groups][16 rows]. k_scale, v_scale: fp32 [Hkv], finite and
  *          > 0, read only.
- * All pointers are device pointers, 16-byte aligned. */
+ * All pointers are device pointers, 16-byte aligned; the scales of E2M1 need only a float's alignment. */
 typedef enum {
   POD_ATTN_KV_BF16 = 0,
   POD_ATTN_KV_E4M3 = 1,

@@ -146,6 +146,20 @@ def test_expand_refusals(lib):
     assert run(_plan(cu_seqlens=[], kv_lens=[9], kv_fp8=True)) == B.ERR_UNSUPPORTED
 
 
+def test_scales_that_are_not_aligned_are_refused(lib):
+    """A float's alignment for the 4-bit cache's scales (4 bytes), 16 bytes for the e4m3 cache's."""
+    bad = B.ERR_INVALID_ARG
+    for kw in (dict(ks=50), dict(vs=66)):
+        c = _desc("e2m1", **kw)
+        assert _rope_append(lib, cache=c) == bad
+        assert lib.pod_attn_run_decode_fp4(_decode_plan().handle, 16, ctypes.byref(c), 16, 16, 16,
+                                           1 << 30, 1 << 30, None) == bad
+        assert lib.pod_attn_expand_fp4(_plan().handle, ctypes.byref(c), 16, 16, 16, 16, 16, 1 << 30,
+                                       1 << 30, None) == bad
+    for kw in (dict(ks=52), dict(vs=68)):
+        assert _rope_append(lib, cache=_desc("e4m3", **kw)) == bad
+
+
 @pytest.mark.parametrize("pairs,ok", [
     ([(0, 9)], True), ([(0, 9), (0, 8)], True), ([(3, 3)], True), ([(3, 3), (3, 4)], True),
     ([(3, 3), (3, 3)], True), ([(0, 10)], False), ([(-1, 2)], False), ([(10, 2)], False),

@@ -222,6 +222,37 @@ def test_serving_over_a_4_bit_cache(hq, hkv, D, rot, interleaved):
     s.step([2, 3, 0])
 
 
+@pytest.mark.parametrize("hkv,layer", [(1, 1), (1, 3), (2, 1), (5, 2)])
+def test_head_scales_in_a_table_of_all_layers(hkv, layer):
+    """A layer's head scales as a row of fp32 [layers][Hkv], at whatever multiple of 4 bytes it starts,
+    give the bits of the same scales in tensors of their own."""
+    c = K.Fp4Case(2 * hkv, hkv, 64, [40, 300], seed=hkv).to()
+    table = torch.full((2, 4, hkv), float("nan"), device="cuda")
+    table[0, layer], table[1, layer] = c.cache.tensors[2], c.cache.tensors[3]
+    rows = torch.randn((2, 4 * hkv, 64), generator=torch.Generator().manual_seed(1))
+    rows = rows.to(torch.bfloat16).cuda()
+    plan = c.plan()
+    wide = B.Plan(2 * hkv, hkv, [], c.lens, 2, c.nb, c.bt.shape[1], .1, head_dim=64)
+    ws, ws16 = plan.alloc_workspace(), wide.alloc_workspace()
+    plan.upload(ws)
+    wide.upload(ws16)
+    got = []
+    for scales in (c.cache.tensors[2:], table[:, layer]):
+        pools = [t.clone() for t in (c.k, c.v)]
+        cache = B.KvCache("e2m1", *pools, *scales)
+        o, q = torch.empty_like(c.qd), torch.empty_like(c.qd)
+        out = [torch.zeros((c.nb, hkv, 16, 64), dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+        plan.rope_append(B.Rope(64), rows[:, :2 * hkv], rows[:, 2 * hkv:3 * hkv], rows[:, 3 * hkv:],
+                         cache, c.tab, None, q, ws)
+        plan.run_decode_fp4(q, cache, c.tab, c.kv, o, ws)
+        wide.expand_fp4(cache, c.tab, *out, c.tab, c.kv, ws16)
+        assert plan.device_status(ws) == B.OK and wide.device_status(ws16) == B.OK
+        got.append(pools + [q, o] + out)
+    assert torch.isfinite(got[0][3]).all()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("graph", [False, True])
 @pytest.mark.parametrize("hq,hkv,D,lens", [
     (32, 8, 128, [700, 31, 2000, 90]), (8, 8, 64, [300] * 20), (8, 1, 128, [30000])])
