@@ -194,7 +194,14 @@ def _check(code, where):
         raise PodAttnError(code, where)
 
 
+def _fits_i32(what: str, values: Sequence[int]):
+    """Refuse whole numbers that an int32 does not hold: ctypes would drop their upper bits."""
+    if values and (min(values) < -(1 << 31) or max(values) >= 1 << 31):
+        raise ValueError(f"{what}: beyond int32 in {values}")
+
+
 def _i32_array(values: Sequence[int]):
+    _fits_i32("list", values)
     arr = (ctypes.c_int32 * max(1, len(values)))(*values)
     return arr
 
@@ -283,6 +290,7 @@ class Rope:
                  high_freq_factor: float = 4.0, attention_factor: float = 0.0,
                  inv_freq: Optional[Sequence[float]] = None):
         self.handle = None
+        _fits_i32("rot_dim", (rot_dim,))
         freq = None
         if inv_freq is not None:
             if scaling != "custom":
@@ -391,6 +399,8 @@ class Pages:
 
     def __init__(self, num_blocks: int, max_seqs: int, max_blocks_per_seq: int):
         self.handle = None
+        _fits_i32("num_blocks, max_seqs, max_blocks_per_seq",
+                  (num_blocks, max_seqs, max_blocks_per_seq))
         handle = ctypes.c_void_p()
         _check(load().pod_attn_pages_create(num_blocks, max_seqs, max_blocks_per_seq,
                                             ctypes.byref(handle)), "pod_attn_pages_create")
@@ -402,6 +412,7 @@ class Pages:
             self.handle = None
 
     def grow(self, seq: int, kv_len: int):
+        _fits_i32("seq, kv_len", (seq, kv_len))
         pair, n = (ctypes.c_int32 * 2)(), ctypes.c_int32()
         _check(load().pod_attn_pages_grow(self.handle, seq, kv_len,
                                           ctypes.cast(pair, ctypes.c_void_p), ctypes.byref(n)),
@@ -409,9 +420,11 @@ class Pages:
         return [tuple(pair)] if n.value else []
 
     def fork(self, src: int, dst: int, kv_len: int):
+        _fits_i32("src, dst, kv_len", (src, dst, kv_len))
         _check(load().pod_attn_pages_fork(self.handle, src, dst, kv_len), "pod_attn_pages_fork")
 
     def free(self, seq: int):
+        _fits_i32("seq", (seq,))
         _check(load().pod_attn_pages_free(self.handle, seq), "pod_attn_pages_free")
 
     def compact(self):
@@ -469,6 +482,9 @@ class Plan:
                  kv_fp4: bool = False):
         lib = load()
         np_ = len(cu_seqlens) - 1 if len(cu_seqlens) > 0 else 0
+        _fits_i32("sizes and options",
+                  (num_q_heads, num_kv_heads, num_decode_seqs, num_blocks, max_blocks_per_seq, num_sms,
+                   ctas_per_sm, max_prefill_ctas, decode_splits, prefill_splits, head_dim))
         self.problem = Problem(num_q_heads, num_kv_heads, head_dim, 16, np_,
                                int(cu_seqlens[-1]) if np_ > 0 else 0, num_decode_seqs,
                                num_blocks, max_blocks_per_seq, scale)

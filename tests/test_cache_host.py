@@ -509,6 +509,22 @@ def test_pages_refusals(lib):
     lib.pod_attn_pages_destroy(None)
 
 
+@pytest.mark.parametrize("off", [1 << 32, -(1 << 32), 1 << 40])
+def test_numbers_beyond_32_bits_are_refused(lib, off):
+    """Not taken modulo 2^32."""
+    p = B.Pages(10, 3, 5)
+    p.grow(0, 20)
+    for f in (lambda: B.Pages(10 + off, 3, 5), lambda: B.Pages(10, 3 + off, 5),
+              lambda: B.Pages(10, 3, 5 + off), lambda: p.grow(0 + off, 21), lambda: p.grow(0, 21 + off),
+              lambda: p.fork(off, 1, 20), lambda: p.fork(0, 1 + off, 20), lambda: p.fork(0, 1, 20 + off),
+              lambda: p.free(off), lambda: p.tables([off]), lambda: B.Rope(64 + off),
+              lambda: _decode_plan(num_blocks=10 + off), lambda: _plan(kv_lens=[9, 7 + off]),
+              lambda: _plan(num_q_heads=4 + off), lambda: _plan(cu_seqlens=[0, 5 + off])):
+        with pytest.raises(ValueError):
+            f()
+    assert p.free_blocks == 8 and p.tables([0, 1])[1].tolist() == [20, 0]
+
+
 # ---------------------------------------------------------------------------------- the oracle
 def test_oracle_formats():
     """The oracle's own tables: the values of both formats and rounding to them."""
