@@ -494,6 +494,9 @@ class Plan:
                                1 if kv_fp4 else 0)
         self.variant = variant
         cu = _i32_array(list(cu_seqlens) if np_ > 0 else [0])
+        if len(kv_lens) < np_ + num_decode_seqs:  # the library reads one for each sequence
+            raise ValueError(f"kv_lens: {len(kv_lens)} for {np_} prefill and {num_decode_seqs} decode "
+                             "sequences")
         kv = _i32_array(list(kv_lens))
         handle = ctypes.c_void_p()
         code = lib.pod_attn_plan(ctypes.byref(self.problem), ctypes.cast(cu, ctypes.c_void_p),

@@ -509,6 +509,13 @@ def test_pages_refusals(lib):
     lib.pod_attn_pages_destroy(None)
 
 
+@pytest.mark.parametrize("kw", [dict(kv_lens=[9]), dict(kv_lens=[]), dict(num_decode_seqs=2),
+                                dict(cu_seqlens=[0, 2, 5])])
+def test_plans_of_more_sequences_than_lengths_are_refused(lib, kw):
+    with pytest.raises(ValueError):
+        _plan(**kw)
+
+
 @pytest.mark.parametrize("off", [1 << 32, -(1 << 32), 1 << 40])
 def test_numbers_beyond_32_bits_are_refused(lib, off):
     """Not taken modulo 2^32."""
