@@ -70,9 +70,10 @@ struct Oct {
 // the Taylor series to x^9 and x^8 are off by 2^-29 and 2^-25, and quarter turns swap and negate.
 // kFine: the radians are x + e, e being what rounding x left (the integer's two parts are exact in fp32, and
 // so are the remainders of the products), and cos has its x^10 term. sin is then good to 0.8 units in the
-// last place instead of 1.4, cos to 1.1 instead of 1.4. e4m3 rows are rotated with it: of a million codes 1.1
-// instead of 1.5 fall on the other side of a tie than in 64 bits, for 2 % (8000 tokens, 8 kv-heads) to 5 %
-// more time. bf16 rows round it away and e2m1 codes do not change with it.
+// last place instead of 1.4, cos to 1.1 instead of 1.4. e4m3 K rows are rotated with it: of a million codes
+// 1.1 instead of 1.5 fall on the other side of a tie than in 64 bits, for about 2 % more time (8000 tokens, 8
+// kv-heads). q is rotated without it whatever the cache; bf16 rows round it away and e2m1 codes do not
+// change with it.
 template <bool kFine>
 __device__ __forceinline__ void angle(uint64_t turn, int pos, float mag, float& c, float& s) {
   constexpr float kUnit = 1.46291807926715968e-9f;  // 2 pi / 2^32
@@ -233,8 +234,13 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas)
     const int a0 = turned ? c0 : 8 * l, a1 = turned ? c1 : 8 * l + 4;
     float c[kAngles], s[kAngles];
     if (turned) {
+      if (KV == POD_ATTN_KV_E4M3 && what == 1) {
 #pragma unroll
-      for (int j = 0; j < kAngles; ++j) angle<KV == POD_ATTN_KV_E4M3>(turn[j], pos, a.mag, c[j], s[j]);
+        for (int j = 0; j < kAngles; ++j) angle<true>(turn[j], pos, a.mag, c[j], s[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kAngles; ++j) angle<false>(turn[j], pos, a.mag, c[j], s[j]);
+      }
     }
     uint16_t* dst;       // bf16 rows: head r at dst + r * pitch
     int64_t pitch = HD;

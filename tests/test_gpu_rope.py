@@ -263,6 +263,16 @@ def test_4_bit_rotated_rows(D, rot, interleaved):
     assert np.array_equal(a, b)
 
 
+@pytest.mark.parametrize("rot,interleaved", [(128, False), (64, True), (84, False)])
+def test_queries_do_not_depend_on_the_cache(rot, interleaved):
+    outs = []
+    for kind in ("bf16", "e4m3", "e2m1"):
+        c = Case(8, 1, 128, [3000], [50000], [1, 70001], seed=15, kind=kind)
+        assert c.run(B.Rope(rot, interleaved=interleaved)) == B.OK
+        outs.append(c.q_out())
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
 # ---------------------------------------------------------------------------------- calls
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "e2m1"])
 def test_bad_block_index_is_reported(kind):
