@@ -7,17 +7,19 @@
 // The work is the plan's shares of decode items (one sequence, one kv-head with its G query heads, a
 // range of 16-row blocks; "LLMSO - W4", §"FlashDecoding — decode 단계의 병렬성 확보"), one for each group
 // of warps: a persistent CTA per SM holds four groups of four, or one of all 16 where outputs are few
-// (the planner chooses). Each warp streams its own (block, kv-head) units into a private ring in shared memory, one bulk copy for the K unit and one for the V unit (codes
-// and scales of 16 rows are contiguous), and keeps an online softmax per head.
+// (the planner chooses). Each warp streams its own (block, kv-head) units into a private ring in shared
+// memory, one bulk copy for the K unit and one for the V unit (codes and scales of 16 rows are
+// contiguous), and keeps an online softmax per head.
 //
 // What bounds it (GB300): 9 * D bytes of a (block, kv-head) take as long to arrive as the SM has to
 // convert and multiply them, 279 instructions at 128 channels: 64 conversions and 16 interleavings (two
 // issue cycles each on the ALU pipe), 64 packed products by the group scales, 16 warp MMAs of 9 cycles.
-// With one query head it is 208 (see fp4_item). Long sequences run at 93 % of the measured copy rate (76 of
-// 16384 rows, 8 kv-heads: 224 us), with one query head at 97 % (213 us); 64 sequences of 8192 to 16384
-// rows take 146 us (89 %), 32 MHA sequences of 2048 to 4096 rows 75 us (89 %), one of 130001 rows of 4
-// kv-heads and 64 channels 20 us (28 %: start, and the merge of 32 partials an output), one of 2^20 rows
-// of 2 kv-heads 63 us (70 %).
+// With one query head it is 208 (see fp4_item). Long sequences run at 94 % of the measured copy rate (76 of
+// 16384 rows, 8 kv-heads: 225 us), with one query head at 98 % (216 us); 64 sequences of 8192 to 16384
+// rows take 146 us (89 %), 32 MHA sequences of 2048 to 4096 rows 75.7 us (88 %), one of 2^20 rows of 2
+// kv-heads 63 us (70 %), one of 130001 rows of 4 kv-heads and 64 channels 19.8 us (28 %): there 128 CTAs take
+// 8 to 11 us over their four rounds each and end 12 us after the first start, then one CTA an output reads
+// and merges 32 partials for 5 us while the others are idle.
 
 #include <cuda_runtime.h>
 

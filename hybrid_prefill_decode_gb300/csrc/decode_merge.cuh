@@ -12,12 +12,14 @@ namespace pod {
 
 using namespace ptx;
 
-// Where a decode item runs: `nw` (= 4) warps from absolute warp `w0`, their rings and score
-// areas, the named barrier of the slot that runs it and the slot's index in the control block.
+// Where a decode item runs: `nw` warps (4; in the 4-bit decode a group's 4 or 16) from absolute warp
+// `w0`, the memory in which they are combined, the named barrier of the slot or group that runs it and
+// its index in the control block.
 struct DecodeCtx {
   int w0, nw;
-  uint8_t* ring;        // nw * kDecodeSlots * kSmemDecodeSlot bytes; also the combine scratch
-  float* scores;        // nw * kMaxGroup * kBlockSize floats
+  uint8_t* ring;        // combine scratch: the warps' rings (nw * kDecodeSlots * kSmemDecodeSlot bytes);
+                        // in the 4-bit decode memory of its own beside them
+  float* scores;        // nw * kMaxGroup * kBlockSize floats; not used by the 4-bit decode
   int bar_id, bar_threads, first_thread, slot;
 };
 
@@ -39,7 +41,7 @@ constexpr int kRow = kHeadDim + 2;  // global partial slot row: o[128], m, l
 // arrive sums the bundle up into the bundle's first slot, the last bundle's sum goes with the others'
 // into the output. Sums go in the splits' order, whoever makes them. kLevels: plans that have such units;
 // the others' kernels leave the second level out, without which their main loop comes out 2 to 3 % faster
-// (64 sequences of 8192 to 16384 rows, 8 kv-heads of 4 heads: 7 us of 155).
+// (64 sequences of 8192 to 16384 rows, 8 kv-heads of 4 heads: 155 -> 150 us when it was left out).
 // A barrier orders the group's partials before the release of the thread that counts the arrival, its
 // acquire (in the last to arrive) the others' before the group's reads.
 template <int GT, int HD, int kGW, bool kLevels, class P, class Ctl>

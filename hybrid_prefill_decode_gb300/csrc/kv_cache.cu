@@ -47,7 +47,7 @@ enum RopeLayout {
   kHalf = 0,         // pairs (i, i + rot / 2), rot a multiple of 8: a lane holds 4 pairs
   kInterleaved = 1,  // pairs (2i, 2i + 1), rot a multiple of 8 (0: no rotation): 8 neighbours, 4 pairs
   kAny = 2           // any even rot, either kind: 8 neighbours, partners through shared memory
-                     // (16384 tokens of 32 + 2 x 4 heads: 117 us, the others 59 and 57 us)
+                     // (16384 tokens of 32 + 2 x 4 heads: 117 us, the others 58 and 55 us)
 };
 
 // Eight channels of one head in fp32 and as they were read.
@@ -65,8 +65,8 @@ struct Oct {
 };
 
 // cos and sin, times the attention factor, of one pair's angle at a position. Position times a 64-bit
-// fraction of a turn wraps around modulo a turn by itself, so far positions lose nothing. Its top 32
-// bits split into the nearest quarter turn and a rest x of at most pi / 4, exact in the integer; there
+// fraction of a turn wraps around modulo a turn by itself, so far positions lose only what the 53 bits of
+// the frequency's quotient by 2 pi leave. Its top 32 bits split into the nearest quarter turn and a rest x of at most pi / 4, exact in the integer; there
 // the Taylor series to x^9 and x^8 are off by 2^-29 and 2^-25, and quarter turns swap and negate.
 // kFine: the radians are x + e, e being what rounding x left (the integer's two parts are exact in fp32, and
 // so are the remainders of the products), and cos has its x^10 term. sin is then good to 0.8 units in the
@@ -167,9 +167,10 @@ __device__ __forceinline__ void store_quantised(const RopeAppendArgs& a, const f
 // lanes each, with the loads of kRopeBatch such steps in flight. The angles of a lane's pairs are
 // computed once per work and serve all its heads. Bound by memory on a bf16 cache (16380 tokens of 32 +
 // 2 x 32 heads, 64 of 128 channels rotated: 118 us from call to call, the measured copy rate; 16384 of 32 + 2
-// x 4: 57 us, 86 %), by the instructions of the quantisation on the others (8000 of 32 + 2 x 8 heads in e4m3:
-// 47.5 us, 57 %; with 4000 of 32 + 2 x 32: 52 us, 46 %). More CTAs an SM with fewer registers, or fewer steps
-// in flight, were slower (16380 tokens: 140 to 157 us).
+// x 4: 58 us, 85 %). Bound by instructions on the others: of 16380 tokens of 32 + 2 x 32 heads the e4m3 cache
+// takes 207 us (48 %), e2m1 214 us (42 %), with an instruction issued in 72 % of the cycles, the ALU pipe busy in
+// 43 to 45 % and the memory at a third (8000 of 32 + 2 x 8 heads in e4m3: 47.7 us, 56 %). More CTAs an SM with
+// fewer registers, or fewer steps in flight, were slower (16380 tokens in bf16: 140 to 157 us).
 constexpr int kRopeBatch = 4;
 constexpr int kRopeWarps = 8;
 constexpr int kRopeCtas = 4;  // CTAs an SM holds
@@ -361,8 +362,10 @@ struct ExpandArgs {
 
 // One warp per K or V unit of a sequence's block. A lane takes eight code bytes at a time, which are one
 // group of 16 channels, and writes their 32 bytes at once, so that every store is a whole sector. Bound
-// by memory: 30720 rows of 4 heads take 13.3 us (80.6 MB, 89 % of the measured copy rate; 22.8 us with
-// 4-byte loads, 16-byte stores and K and V in one warp).
+// by memory: 30720 rows of 4 heads take 15 us (80.6 MB, 79 % of the measured copy rate; 4-byte loads,
+// 16-byte stores and K and V in one warp took 9 us more). A grid row per sequence, as wide as the longest
+// one asks for: CTAs beyond a sequence's end read its length and leave, which costs most where one long
+// sequence stands beside many short ones (30720 rows and 256 times 40: 172 us of a floor of 16).
 template <int HD>
 __global__ void __launch_bounds__(256) expand_fp4_kernel(const __grid_constant__ ExpandArgs a) {
   constexpr int kSteps = HD / 32;  // groups of a lane
@@ -420,7 +423,8 @@ __global__ void __launch_bounds__(256) expand_fp4_kernel(const __grid_constant__
 // ============================================================================ block copies
 // One CTA per pair and pool; the pools and the pairs of one launch are in its parameters (the device has
 // nothing to read first, and nothing has to outlive the call). Bound by memory: 1201 blocks of 16 KiB in
-// 16 pools take 92 us from call to call, the measured copy rate.
+// 16 pools take 92 us from call to call, the measured copy rate. Few pairs of very large blocks are bound by
+// what one SM moves (four of 1 MiB in two pools: 22 us of a floor of 2.5).
 template <int POOLS, int PAIRS>
 struct CopyArgs {
   struct {

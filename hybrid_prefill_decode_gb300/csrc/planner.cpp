@@ -263,10 +263,11 @@ Shares cut_shares(const std::vector<int64_t>& nblks, int64_t groups, int64_t rou
   return cut;
 }
 
-// About how long shares take (in 1/20 us) in groups of `warps` warps, pairs pairs of channels an output.
-// A round of four warps takes 0.65 us alone and 0.45 for each of the SM's groups when they share it, one of
-// 16 warps 1.9; to this an item's start and the merge. (Fitted to 129 batches of 1 to 76 sequences of 64 to
-// 131072 rows, 64 and 128 channels, 1 to 8 heads: 11 % off on average.)
+// About how long shares take (in 1/20 us, without the launch) in groups of `warps` warps, pairs pairs of
+// channels an output. A round of four warps takes 0.65 us alone and 0.45 for each of the SM's groups when
+// they share it, one of 16 warps 1.9; to this an item's start and the merge. Of 176 batches of 1 to 76
+// sequences of 64 to 131072 rows (64 and 128 channels, 1 to 8 heads) the choice between the two groups takes
+// 0.7 % more than the better one on average and 12 % at worst, and 5.9 % less than groups of four always.
 int64_t fp4_time(const Shares& cut, int64_t num_sms, int64_t round, int warps, int pairs) {
   const bool wide = warps == kFp4Warps;
   const int64_t shares = (int64_t)cut.starts.size() - 1;

@@ -1429,7 +1429,7 @@ __device__ void decode_item(const Params& p, const CUtensorMap* tmk, const CUten
   } else {
     decode_tc<GT, HD>(p, tmk, tmv, it, dc, ctl, ps, wc);
   }
-  combine_decode<GT, HD, false>(p, d, g, unit, split, dc, ctl, 1.f);
+  combine_decode<GT, HD>(p, d, g, unit, split, dc, ctl, 1.f);
 }
 
 // ============================================================================ scheduler

@@ -363,7 +363,9 @@ typedef struct {
 typedef struct pod_attn_rope_s* pod_attn_rope_t;
 
 /* Make a host handle holding the frequencies of `config` (copied; no device memory). They are kept
- * as 64-bit fractions of a turn per position, so angles are exact modulo a turn at any position.
+ * as 64-bit fractions of a turn per position: at position p an angle is off by at most p * f / 2 pi *
+ * 2^-52 turns (the quotient f / 2 pi in 53 bits), 2^-32 turns (what a launch keeps of the product) and
+ * 2^-23 radians (what is left modulo a quarter turn, in fp32).
  * Read only after this call: any number of threads and streams may use it.
  * Errors: INVALID_ARG (nulls, a parameter outside its range). */
 pod_attn_status pod_attn_rope_create(const pod_attn_rope_config* config, pod_attn_rope_t* out);
@@ -420,7 +422,8 @@ pod_attn_status pod_attn_rope_append(pod_attn_plan_t plan, pod_attn_rope_t rope,
  * (with one query head per kv-head also their products with V's scale bytes) are rounded to f16;
  * scores, softmax statistics and accumulation are fp32. A NaN or an infinity in a query head makes
  * that head's outputs NaN, and a cached NaN (scale byte 0x7F) in a visible row its sequence's outputs
- * where the formula does.
+ * where the formula does. Scores (q k scale) are taken to be below 2^23 in magnitude: beyond, fp32
+ * holds no fractions of them, and a weight may pass f16's range and give NaN.
  *   plan  : a plan made with options.kv_fp4 and no prefill sequences (else UNSUPPORTED); its variant
  *           is not used: the work runs as one launch.
  *   cache : type E2M1 (else UNSUPPORTED); num_blocks as in the plan's problem (else INVALID_ARG).
