@@ -6,6 +6,7 @@ import torch
 
 import cache_cases as K
 from hybrid_prefill_decode_gb300 import binding as B
+from hybrid_prefill_decode_gb300 import workloads as W
 from oracle import cache_ops as C
 
 pytestmark = pytest.mark.gpu
@@ -312,6 +313,72 @@ def test_launches_one_behind_another_see_each_others_writes(hq, hkv, D, lens, gr
         assert torch.equal(outs[0].view(torch.int16), outs[1].view(torch.int16))
         for a, b in zip(c.cache.tensors + pools, want):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("variant", ["fused", "serial", "streams"])
+def test_launches_among_those_of_the_attention(variant, graph):
+    """The attention's launches (with the append in front one that needs all its CTAs at once, or several
+    on two streams) between the cache operators': the bits of the same run with a wait behind each."""
+    b = W.make_batch(8, 2, [60, 7], [200, 300], [900, 31], seed=5, device="cuda")
+    plan = B.Plan.for_batch(b, variant=variant)
+    ws = plan.alloc_workspace()
+    plan.upload(ws)
+    rope, cache = B.Rope(128), B.KvCache("bf16", b.k_pool, b.v_pool)
+    used = set()
+    for i, n in enumerate([200, 300, 900, 31]):
+        used |= set(b.block_tables[i, :-(-n // 16)].tolist())
+    spare = sorted(set(range(b.num_blocks)) - used)[0]
+    move = [(int(b.block_tables[2, 3]), spare), (spare, int(b.block_tables[3, 0]))]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rows = torch.randn((5, 69, 12, 128), generator=g, device="cuda").to(torch.bfloat16)
+    buf, k_new = torch.empty_like(rows[0]), torch.empty((2, 69, 2, 128), dtype=torch.bfloat16,
+                                                        device="cuda")
+    qp, qd = torch.empty_like(b.q_prefill), torch.empty_like(b.q_decode)
+    outs = [[torch.empty((5, 2) + t.shape, dtype=t.dtype, device="cuda") for t in (qp, qd)]
+            for _ in range(2)]
+    clean, side = [b.k_pool.clone(), b.v_pool.clone()], torch.cuda.Stream()
+
+    def run(out, wait):
+        b.k_pool.copy_(clean[0])
+        b.v_pool.copy_(clean[1])
+        for i in range(5):
+            buf.copy_(rows[i])
+            k_new[0].copy_(rows[i, :, 8:10])
+            k_new[1].copy_(rows[i, :, 10:])
+            wait()
+            plan.rope_append(rope, buf[:, :8], buf[:, 8:10], buf[:, 10:], cache, b.block_tables, qp, qd,
+                             ws)
+            wait()
+            plan.run(qp, qd, b.k_pool, b.v_pool, b.block_tables, b.cu_seqlens_q, b.kv_lens,
+                     out[0][i, 0], out[1][i, 0], ws, stream2=side)
+            wait()
+            B.copy_blocks([b.k_pool, b.v_pool], move[:1])
+            wait()
+            plan.run_append(qp, qd, k_new[0], k_new[1], b.k_pool, b.v_pool, b.block_tables,
+                            b.cu_seqlens_q, b.kv_lens, out[0][i, 1], out[1][i, 1], ws, stream2=side)
+            wait()
+            B.copy_blocks([b.k_pool, b.v_pool], move[1:])
+            wait()
+
+    main = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main):
+        run(outs[0], torch.cuda.synchronize)
+        want = [b.k_pool.clone(), b.v_pool.clone()]
+        torch.cuda.synchronize()
+        if graph:
+            with torch.cuda.graph(gr := torch.cuda.CUDAGraph(), stream=main):
+                run(outs[1], lambda: None)
+        for _ in range(10):
+            for t in outs[1]:
+                t.zero_()
+            gr.replay() if graph else run(outs[1], lambda: None)
+            torch.cuda.synchronize()
+            assert plan.device_status(ws) == B.OK
+            assert all(torch.isfinite(t).all() for t in outs[0])
+            for x, y in zip(outs[0] + want, outs[1] + [b.k_pool, b.v_pool]):
+                assert torch.equal(x.view(torch.int16), y.view(torch.int16))   # rows of no one: NaN
 
 
 @pytest.mark.parametrize("graph", [False, True])

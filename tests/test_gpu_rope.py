@@ -118,6 +118,21 @@ def test_rotary_dims_of_two():
         _check_rotated(c.q_out(), c.q, c.pos, 2, interleaved, {})
 
 
+@pytest.mark.parametrize("rot,interleaved", [(64, False), (64, True), (42, False)])
+def test_frequencies_of_the_caller_s(rot, interleaved):
+    """Negative ones, zero, some beyond a turn per position, and an attention factor."""
+    freq = np.random.default_rng(rot).uniform(-9, 9, rot // 2)
+    freq[:3] = 0.0, -0.0, 2 * np.pi
+    c = Case(3, 1, 64, [40], [300], [1, 70000], seed=16)
+    rope = B.Rope(rot, interleaved=interleaved, scaling="custom", inv_freq=freq.tolist(),
+                  attention_factor=1.5)
+    assert c.run(rope) == B.OK
+    want, size = C.rotate(K.f64(c.q), c.pos, freq, 1.5, rot, interleaved)
+    # as _check_rotated's; 70000 positions of 1.5 turns each lose 2^-34 turns of their quotient
+    err = np.abs(K.f64(c.q_out()) - want)
+    assert (err <= 2.0 ** -8 * np.abs(want) + 2.0 ** -20 * size).all()
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_far_positions(interleaved):
     """Positions around 2^24 (beyond which fp32 does not hold every whole number) and 2^26."""
@@ -214,6 +229,20 @@ def test_e4m3_cache_equals_the_existing_append():
     assert plan.device_status(ws) == B.OK
     assert np.array_equal(d.k8.cpu().numpy(), k8) and np.array_equal(d.v8.cpu().numpy(), v8)
     assert np.array_equal(d.v_scale.cpu().numpy(), vs, equal_nan=True)
+
+
+@pytest.mark.parametrize("rot,interleaved", [(128, True), (64, False), (84, False), (42, True)])
+def test_e4m3_rotated_rows_in_every_layout(rot, interleaved):
+    """As test_e4m3_rotated_rows, K only."""
+    c = Case(4, 2, 128, [60], [100], [1, 5000], seed=17, kind="e4m3")
+    assert c.run(B.Rope(rot, interleaved=interleaved)) == B.OK
+    freq, mag = C.rope_frequencies(rot)
+    want, size = C.rotate(K.f64(c.k), c.pos, freq, mag, rot, interleaved)
+    ks = c.scales[0].cpu().numpy().astype(np.float64)
+    got = K.f64(c.pools[0])[c.blk, :, c.row] * ks
+    want = np.clip(want, -448 * ks, 448 * ks)
+    assert (np.abs(got - want) <= 2.0 ** -4 * np.abs(want) + (2.0 ** -10 + 2.0 ** -14) * ks +
+            2.0 ** -19 * size).all()
 
 
 def test_e4m3_rotated_rows():
