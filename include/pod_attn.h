@@ -601,7 +601,7 @@ pod_attn_status pod_attn_read_records(pod_attn_plan_t plan, const void* workspac
  * serialise them. Device-detected errors (bad block index, timeout) are recorded in the
  * array's status word: read them with pod_attn_last_device_status(plan, NULL, stream).
  * Errors: INVALID_ARG (null plan, variant other than FUSED, an instrumented plan, a stream of
- * another device, null/misaligned tensors), UNSUPPORTED (a plan for the e4m3 cache), WORKSPACE
+ * another device, null/misaligned tensors), UNSUPPORTED (a plan for the e4m3 or e2m1 cache), WORKSPACE
  * (plan needs more than POD_ATTN_STATIC_SCRATCH_BYTES), CUDA. */
 #define POD_ATTN_STATIC_SCRATCH_BYTES (32u * 1024u * 1024u)
 pod_attn_status pod_attn_run_static(pod_attn_plan_t plan, const void* q_prefill,
