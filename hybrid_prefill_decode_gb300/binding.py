@@ -197,7 +197,7 @@ def _check(code, where):
 def _fits_i32(what: str, values: Sequence[int]):
     """Refuse whole numbers that an int32 does not hold: ctypes would drop their upper bits."""
     if values and (min(values) < -(1 << 31) or max(values) >= 1 << 31):
-        raise ValueError(f"{what}: beyond int32 in {values}")
+        raise ValueError(f"{what}: {min(values)} to {max(values)} is beyond int32")
 
 
 def _i32_array(values: Sequence[int]):

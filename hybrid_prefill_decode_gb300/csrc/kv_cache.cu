@@ -66,8 +66,9 @@ struct Oct {
 
 // cos and sin, times the attention factor, of one pair's angle at a position. Position times a 64-bit
 // fraction of a turn wraps around modulo a turn by itself, so far positions lose only what the 53 bits of
-// the frequency's quotient by 2 pi leave. Its top 32 bits split into the nearest quarter turn and a rest x of at most pi / 4, exact in the integer; there
-// the Taylor series to x^9 and x^8 are off by 2^-29 and 2^-25, and quarter turns swap and negate.
+// the frequency's quotient by 2 pi leave. Its top 32 bits split into the nearest quarter turn and a rest x of
+// at most pi / 4, exact in the integer; there the Taylor series to x^9 and x^8 are off by 2^-29 and 2^-25,
+// and quarter turns swap and negate.
 // kFine: the radians are x + e, e being what rounding x left (the integer's two parts are exact in fp32, and
 // so are the remainders of the products), and cos has its x^10 term. sin is then good to 0.8 units in the
 // last place instead of 1.4, cos to 1.1 instead of 1.4. e4m3 K rows are rotated with it: of a million codes

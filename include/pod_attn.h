@@ -401,10 +401,10 @@ pod_attn_status pod_attn_rope_frequencies(pod_attn_rope_t rope, double* out,
  *               reads them. They may be the memory of q itself (q contiguous, q_stride Hq * D,
  *               q_prefill = q, q_decode = q + T_p * Hq * D), else must not overlap q, k_new or v_new.
  * Rotation is computed in fp32 and rounded once, to bf16 or to the cache's type; q's rows are the same
- * bits whatever the cache. Asynchronous on `stream`; capturable. Tokens that share a cache row (block tables that map two sequences to one
- * block) leave one of their rows there, which one is not defined. A block-table entry outside
- * [0, cache->num_blocks) is reported as BAD_INDEX in the workspace status word; that row is not
- * written.
+ * bits whatever the cache. Asynchronous on `stream`; capturable. Tokens that share a cache row (block
+ * tables that map two sequences to one block) leave one of their rows there, which one is not defined.
+ * A block-table entry outside [0, cache->num_blocks) is reported as BAD_INDEX in the workspace status
+ * word; that row is not written.
  * Errors: INVALID_ARG (nulls, misalignment, strides, overlap, rot_dim beyond the head dim),
  * UNSUPPORTED (E4M3 with another head dim), WORKSPACE, CUDA. */
 pod_attn_status pod_attn_rope_append(pod_attn_plan_t plan, pod_attn_rope_t rope, const void* q,
